@@ -25,13 +25,18 @@
 // codes). Q goes to FP16 times a power of two per row that puts the row's maximum in
 // [2^14, 2^15): exact for all but elements 2^-29 below the maximum, which lose bits
 // 2^-39 below it. A key's power of two multiplies its FP32 score. A value's goes into
-// P: P' = 2^(s c - m) * 2^(ev - E + 14) with E the largest exponent of the warp's keys
-// so far, so P' <= 2^14 and FP16 holds 2^-38 of the largest weight; O is scaled back
-// by 2^(E - 14) in FP32. The sum l takes P itself.
+// P, whose FP16 has no room for values of any size: a warp takes its keys of a tile in
+// bands. A band is the keys that some row sees whose exponent is at most 12 below the largest
+// one left, E; P' = 2^(s c - x) * 2^(ev - E + 14) with x the row's largest score in the band,
+// so P' <= 2^14 and FP16 holds weights to 2^-27 of the band's largest, whatever weight or size
+// other keys have. The band's products come out of the MMAs by themselves and are added
+// to O in FP32 times 2^(x - m) 2^(E - 14); l takes its sum times 2^(x - m). Values within
+// 2^12 of each other, the usual case, are one band and one pass.
 //
-// Measured (8 KV heads): one token of 16 sequences of 8192 keys, E4M3, d = 128, 51 us (271 MB
-// at 5.3 TB/s, 78 % of a copy's rate); one of 64 sequences, window 1024, FP16, d = 64, 38 us
-// (132 MB at 3.5 TB/s: 1.7 units a CTA, so starting, borders and merging weigh as much).
+// Measured (8 KV heads): one token of 16 sequences of 8192 keys, 4 heads a KV head, E4M3,
+// d = 128, 52 us (271 MB at 5.2 TB/s, 77 % of a copy's rate), two tokens of 8 heads 68 us; one
+// of 64 sequences, window 1024, FP16, d = 64, 38 us (132 MB at 3.5 TB/s: 1.7 units a CTA,
+// so starting, borders and merging weigh as much).
 #include "fa_serving.cuh"
 
 #include <cmath>
@@ -265,6 +270,9 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
                          const ExtendParams p) {
   using C = FewCfg<D, FP8, NB>;
   constexpr Elem M = FP8 ? Elem::F16 : E;   // type of the MMAs' operands
+  // the scores are wanted again for a second band, which is rare: with 16 rows of 128 columns
+  // their registers are needed before (16 x 8192 keys: 68 us, with them kept there 75)
+  constexpr bool kPark = FP8 && NB == 2 && D == 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -434,7 +442,6 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
     // the tiles that some row sees only in part: positions of the unit's first and last token
     const int pos_lo = u.s.p0, pos_hi = u.s.p0 + u.s.n - 1;
     float mrow[NB][2], lrow[NB][2];
-    int eref = 0;   // E4M3: exponent byte that O is held against (0: none yet)
     float oacc[D / 16][NB][4];   // O^T: 16 columns by 8 rows each
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -517,38 +524,15 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(stK));
       const int left_keys = u.s.len - key0;   // keys of the tile that exist (a mask cuts the rest)
-      uint32_t vb[2][2];   // V's exponent bytes (0: past the sequence's end)
-      float rise = 1.f;
-      if constexpr (FP8) {
-        // V's exponents: the reference rises to the largest of this warp's keys
-        ok = mbar_wait_w(full(stV), phV, s_abort, p.status);
-        if (!ok) continue;
-        const uint32_t ev = sb + C::kOffExp + stV * C::kExpBytes + kw + kg;
-        uint32_t top = 0;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            vb[mt][h] = kw + 16 * mt + 8 * h + kg < left_keys ? ld_shared_u8x(ev + 16 * mt + 8 * h) : 0u;
-            top = max(top, vb[mt][h]);
-          }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if ((int)top > eref) {   // O so far shrinks by 2^(old - new)
-          rise = eref == 0 ? 0.f : __uint_as_float((uint32_t)max(127 + eref - (int)top, 0) << 23);
-          eref = (int)top;
-        }
-      }
-      // ---- online softmax over this warp's keys; key (relative to the tile) is seen iff
-      // key < hi and (key >= lo or key < snk)
+      const uint32_t tv = sb + stV * C::kTileBytes;
+      // ---- the mask: key (relative to the tile) is seen iff key < hi and (key >= lo or key < snk)
       const int snk = p.sinks - key0;
       const bool cut = key0 + kPage - 1 > pos_lo || (p.window > 0 && key0 <= pos_hi - p.window && snk < kPage);
-      float mx[NB][2];
-      bool up = FP8 && rise != 1.f;
+      if (cut) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (cut) {
+          for (int e = 0; e < 2; ++e) {
             const int hi = pos[nb][e] + 1 - key0;
             const int lo = p.window > 0 ? hi - p.window : -kPage;
 #pragma unroll
@@ -559,62 +543,11 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
                 if (!(key < hi && (key >= lo || key < snk))) sacc[nb][mt][2 * h + e] = -INFINITY;
               }
           }
-          float x = fmaxf(fmaxf(sacc[nb][0][e], sacc[nb][0][2 + e]), fmaxf(sacc[nb][1][e], sacc[nb][1][2 + e]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          mx[nb][e] = fmaxf(mrow[nb][e], x * crow[nb][e]);   // (-inf stays -inf: crow > 0)
-          up |= mx[nb][e] > mrow[nb][e];
-        }
-      // O is touched only where a maximum (or the exponent reference) rose in some row
-      if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // (0 from -inf: nothing was summed yet)
-            const float alpha = mx[nb][e] > mrow[nb][e] ? ex2_approx(mrow[nb][e] - mx[nb][e]) : 1.f;
-            mrow[nb][e] = mx[nb][e];
-            lrow[nb][e] *= alpha;
-            const float shrink = FP8 ? alpha * rise : alpha;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              oacc[i][nb][e] *= shrink;
-              oacc[i][nb][2 + e] *= shrink;
-            }
-          }
       }
-      uint32_t pb[2][NB][2];   // P^T as B operands: keys 16 mt + 8 h .., rows 8 nb ..
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float x[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float mb = mrow[nb][e] == -INFINITY ? 0.f : mrow[nb][e];
-              x[e] = ex2_approx(fmaf(sacc[nb][mt][2 * h + e], crow[nb][e], -mb));
-              lrow[nb][e] += x[e];   // this lane's keys; the eight lanes of a row are added at the end
-            }
-            if constexpr (FP8) {
-              // 2^(14 + byte - reference), 0 where that underflows (and past the end)
-              const float f = __uint_as_float((uint32_t)max((int)vb[mt][h] + (141 - eref), 0) << 23);
-              x[0] *= f;
-              x[1] *= f;
-            }
-            pb[mt][nb][h] = transpose8(pack2<M>(x[0], x[1]));
-          }
-      }
-      if constexpr (!FP8) {
-        ok = mbar_wait_w(full(stV), phV, s_abort, p.status);
-        if (!ok) continue;
-      }
-      const uint32_t tv = sb + stV * C::kTileBytes;
-      // rows past the sequence's end may hold anything, NaN included, and 0 * NaN is
+      // V rows past the sequence's end may hold anything, NaN included, and 0 * NaN is
       // NaN: zero them (each warp its own keys)
-      if (left_keys < kPage) {
+      auto zero_past_end = [&] {
+        if (left_keys >= kPage) return;
         constexpr int kCh = D * (FP8 ? 1 : 2) / 16;
         for (int i = lane; i < 32 * kCh; i += 32) {
           const int key = kw + i / kCh;
@@ -622,33 +555,189 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
         }
         fence_proxy_async_smem();   // before the slot's next TMA load
         __syncwarp();
+      };
+      // E4M3: V's exponent bytes plus 1; 0 for keys of a band before, and for keys that no row of
+      // the unit sees (a row's window begins no earlier than the first one's), which must
+      // not shift the others
+      [[maybe_unused]] uint32_t vb[2][2] = {};
+      if constexpr (FP8) {
+        ok = mbar_wait_w(full(stV), phV, s_abort, p.status);
+        if (!ok) continue;
+        const uint32_t ev = sb + C::kOffExp + stV * C::kExpBytes + kw + kg;
+        const int hi = pos_hi + 1 - key0, lo = p.window > 0 ? pos_lo + 1 - key0 - p.window : -kPage;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = kw + 16 * mt + 8 * h + kg;
+            vb[mt][h] = key < hi && (key >= lo || key < snk) ? ld_shared_u8x(ev + 16 * mt + 8 * h) + 1 : 0u;
+          }
+        zero_past_end();
       }
-      // ---- O^T += V^T P^T
-      const int i = lane >> 3, rr = lane & 7;
+      // ---- online softmax over this warp's keys, and O^T += V^T P^T; E4M3: band by band
+      for (;;) {
+        [[maybe_unused]] uint32_t top = 0, least = 0;   // E4M3: E + 1, and the band's lowest
+        if constexpr (FP8) {
+          top = __reduce_max_sync(0xffffffffu, max(max(vb[0][0], vb[0][1]), max(vb[1][0], vb[1][1])));
+          if (top == 0) break;
+          least = top > 12 ? top - 12 : 1;
+          if constexpr (kPark) {   // the scores wait in the buffers of the unit's end, idle by now
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int dp = 0; dp < (FP8 ? D / 32 : D / 16); ++dp) {
-          uint32_t av[4];
-          if constexpr (FP8) {
+              for (int mt = 0; mt < 2; ++mt)
+                st_shared_v4(sb + C::kOffBuf + ((nb * 2 + mt) * kFewConsumers + threadIdx.x) * 16, __float_as_uint(sacc[nb][mt][0]),
+                             __float_as_uint(sacc[nb][mt][1]), __float_as_uint(sacc[nb][mt][2]), __float_as_uint(sacc[nb][mt][3]));
+          }
+        }
+        auto in_band = [&](int mt, int h) { return !FP8 || vb[mt][h] >= least; };
+        float mx[NB][2];
+        [[maybe_unused]] float xb[NB][2];   // E4M3: the band's largest score of each row
+        bool up = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (in_band(mt, h)) x = fmaxf(x, sacc[nb][mt][2 * h + e]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x *= crow[nb][e];   // (-inf stays -inf: crow > 0)
+            if constexpr (FP8) xb[nb][e] = x;
+            mx[nb][e] = fmaxf(mrow[nb][e], x);
+            up |= mx[nb][e] > mrow[nb][e];
+          }
+        // O is touched only where a maximum rose in some row
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // (0 from -inf: nothing was summed yet)
+              const float alpha = mx[nb][e] > mrow[nb][e] ? ex2_approx(mrow[nb][e] - mx[nb][e]) : 1.f;
+              mrow[nb][e] = mx[nb][e];
+              lrow[nb][e] *= alpha;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                oacc[i][nb][e] *= alpha;
+                oacc[i][nb][2 + e] *= alpha;
+              }
+            }
+        }
+        uint32_t pb[2][NB][2];   // P^T as B operands: keys 16 mt + 8 h .., rows 8 nb ..
+        [[maybe_unused]] float gain[NB][2];   // E4M3: what the band's products count for in O
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          float ref[2], sum[2] = {0.f, 0.f};   // what the scores are held against, and their sum
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            ref[e] = FP8 ? xb[nb][e] : mrow[nb][e];
+            if (ref[e] == -INFINITY) ref[e] = 0.f;
+          }
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float x[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                x[e] = in_band(mt, h) ? ex2_approx(fmaf(sacc[nb][mt][2 * h + e], crow[nb][e], -ref[e])) : 0.f;
+                if constexpr (FP8) sum[e] += x[e];
+                else lrow[nb][e] += x[e];   // this lane's keys; the eight lanes of a row are added at the end
+              }
+              if constexpr (FP8) {   // 2^(14 + byte - E)
+                const float f = in_band(mt, h) ? __uint_as_float((141u + vb[mt][h] - top) << 23) : 0.f;
+                x[0] *= f;
+                x[1] *= f;
+              }
+              pb[mt][nb][h] = transpose8(pack2<M>(x[0], x[1]));
+            }
+          if constexpr (FP8)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = xb[nb][e] == -INFINITY ? 0.f : ex2_approx(xb[nb][e] - mrow[nb][e]);
+              lrow[nb][e] += sum[e] * f;   // (a NaN among the band's scores makes its sum one)
+              // O is held times 2^8, so that 2^(E - 14) stays a normal number down to the
+              // smallest byte that fa_cache_append writes (top = 8)
+              gain[nb][e] = f * __uint_as_float(top > 7 ? (top - 7) << 23 : 0x00400000u >> (7 - top));
+            }
+        }
+        if constexpr (!FP8) {
+          ok = mbar_wait_w(full(stV), phV, s_abort, p.status);
+          if (!ok) break;
+          zero_past_end();
+        }
+        // ---- O^T += V^T P^T
+        const int i = lane >> 3, rr = lane & 7;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int dp = 0; dp < D / 32; ++dp) {
             // 8 x 8 blocks of code pairs, transposed: a lane gets two keys' codes of two
             // adjacent columns; the bytes sorted by column are rows g (even columns of the
             // 16) and g + 8 (odd ones) of an A operand
-            ldmatrix_x4_t(tv + tile_at<D, FP8>(kw + 16 * mt + 8 * (i & 1) + key_of_row<D, FP8>(rr), 2 * dp + (i >> 1)), av);
+            uint32_t av[2][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+              ldmatrix_x4_t(tv + tile_at<D, FP8>(kw + 16 * mt + 8 * (i & 1) + key_of_row<D, FP8>(rr), 2 * dp + (i >> 1)), av[mt]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              uint32_t a[4];
-              e4m3x4_to_f16x2x2(__byte_perm(av[2 * x], 0, 0x3120), a[0], a[1]);
-              e4m3x4_to_f16x2x2(__byte_perm(av[2 * x + 1], 0, 0x3120), a[2], a[3]);
+              float acc[NB][4];   // the band's own products
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb) mma_16816<M>(oacc[2 * dp + x][nb], a, pb[mt][nb][0], pb[mt][nb][1]);
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nb][e] = 0.f;
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                uint32_t a[4];
+                e4m3x4_to_f16x2x2(__byte_perm(av[mt][2 * x], 0, 0x3120), a[0], a[1]);
+                e4m3x4_to_f16x2x2(__byte_perm(av[mt][2 * x + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_16816<M>(acc[nb], a, pb[mt][nb][0], pb[mt][nb][1]);
+              }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  oacc[2 * dp + x][nb][e] = fmaf(acc[nb][e], gain[nb][e & 1], oacc[2 * dp + x][nb][e]);
             }
-          } else {
-            ldmatrix_x4_t(tv + tile_at<D, FP8>(kw + 16 * mt + 8 * (i >> 1) + rr, 2 * dp + (i & 1)), av);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) mma_16816<M>(oacc[dp][nb], av, pb[mt][nb][0], pb[mt][nb][1]);
           }
+          bool rest = false;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (in_band(mt, h)) vb[mt][h] = 0;
+              rest |= vb[mt][h] != 0;
+            }
+          if (!__any_sync(0xffffffffu, rest)) break;
+          if constexpr (kPark) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                const float4 w = ld_shared_v4f(sb + C::kOffBuf + ((nb * 2 + mt) * kFewConsumers + threadIdx.x) * 16);
+                sacc[nb][mt][0] = w.x; sacc[nb][mt][1] = w.y; sacc[nb][mt][2] = w.z; sacc[nb][mt][3] = w.w;
+              }
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int dp = 0; dp < D / 16; ++dp) {
+              uint32_t av[4];
+              ldmatrix_x4_t(tv + tile_at<D, FP8>(kw + 16 * mt + 8 * (i >> 1) + rr, 2 * dp + (i & 1)), av);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma_16816<M>(oacc[dp][nb], av, pb[mt][nb][0], pb[mt][nb][1]);
+            }
+          break;
         }
+      }
+      if (!ok) continue;
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(stV));
     }
@@ -665,7 +754,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
           st_shared_v2(mls + (warp * 16 + 8 * nb + 2 * t + e) * 8, __float_as_uint(mrow[nb][e]), __float_as_uint(lrow[nb][e]));
       }
     const bool all_ok = named_bar_and(1, kFewConsumers, ok);
-    const float back = FP8 ? scalbnf(1.f, eref - 127 - 14) : 1.f;
+    constexpr float back = FP8 ? 1.f / 256.f : 1.f;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
