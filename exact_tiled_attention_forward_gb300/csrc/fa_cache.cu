@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_kernel(const CachePara
         const int b = seq_of(tok[x], r.B, cu);
         const int e = max(cu(b + 1), cu(b));
         const int pos = len_at(r, b) - (e - tok[x]);
-        const int pg = pos >= 0 ? page_at(r, b, pos / kPage) : -1;
+        const int pg = pos >= 0 && pos < r.max_pages * kPage ? page_at(r, b, pos / kPage) : -1;
         if (pg >= 0) at[x] = ((long long)pg * r.H_kv + h) * kPage + pos % kPage;
       }
     }
@@ -240,8 +240,9 @@ int check_ragged(int B, int T, int H_kv, int num_pages, int max_pages, int d, in
   if (cache_format != FA_CACHE_16BIT && cache_format != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || H_kv < 1 || num_pages < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  // positions, table offsets and (page, head) slabs are 32-bit inside the kernels
-  if ((long long)max_pages * kPage >= (1ll << 31) || (long long)B * max_pages >= (1ll << 31) ||
+  // positions (of the rows past the last token of a tile too), table offsets and (page, head)
+  // slabs are 32-bit inside the kernels
+  if ((long long)max_pages * kPage + T >= (1ll << 31) - 256 || (long long)B * max_pages >= (1ll << 31) ||
       (long long)num_pages * H_kv >= (1ll << 31) || (long long)T * H_kv >= (1ll << 31))
     return FA_ERR_INVALID_ARG;
   return FA_OK;

@@ -29,6 +29,7 @@ bool tile_setup(TileParams& t, int d, int format) {
     t.max_split_items = (int)(16 * units < cap ? 16 * units : cap);
   t.grid = (int)(units > t.max_split_items ? units : t.max_split_items);
   t.kv_bytes = 2 * d * (format == FA_CACHE_E4M3 ? 1 : 2);
+  t.key_tiles = paged ? r.max_pages : 0x7FFFFFFF;
   return true;
 }
 

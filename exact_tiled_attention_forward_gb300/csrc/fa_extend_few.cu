@@ -163,7 +163,7 @@ __device__ __forceinline__ int tiles_of(const ExtendParams& p, int b) {
   const SeqTokens s = seq_tokens(p, b);
   if (s.n == 0) return 0;
   // (rows that see no key still get O = 0 and LSE = -inf: one fully masked tile)
-  return max(key_tiles_of(s.p0, s.p0 + s.n, p.window, p.sinks).count(), 1);
+  return max(key_tiles_of(s.p0, s.p0 + s.n, p.window, p.sinks, p.r.max_pages).count(), 1);
 }
 
 // The range of CTA i of n. Every warp works it out by itself, 128 sequences at a time
@@ -242,7 +242,7 @@ struct FewUnit {
 };
 __device__ __forceinline__ void unit_load(const ExtendParams& p, FewUnit& u) {
   u.s = seq_tokens(p, u.b);
-  u.kt = key_tiles_of(u.s.p0, u.s.p0 + u.s.n, p.window, p.sinks);
+  u.kt = key_tiles_of(u.s.p0, u.s.p0 + u.s.n, p.window, p.sinks, p.r.max_pages);
   u.count = max(u.kt.count(), 1);
 }
 __device__ __forceinline__ void unit_first(const ExtendParams& p, const FewRange& fr, FewUnit& u) {
@@ -386,7 +386,6 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
     // ---- Q^T as B operands (query row 8 nb + g, zero past R), and the rows' factors
     uint32_t qb[NB][D / 16][2];
     float crow[NB][2];   // scale log2(e), and the row's power of two undone
-    int pos[NB][2];      // position of the row (below every key for rows past R)
     if (ok) ok = mbar_wait_w(q_full, (uint32_t)units & 1u, s_abort, p.status);
     ++units;
 #pragma unroll
@@ -430,11 +429,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
           }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        crow[nb][e] = __shfl_sync(0xffffffffu, cg, (2 * t + e) * 4);
-        const int r = 8 * nb + 2 * t + e;
-        pos[nb][e] = r < R ? u.s.p0 + r / p.G : -1;
-      }
+      for (int e = 0; e < 2; ++e) crow[nb][e] = __shfl_sync(0xffffffffu, cg, (2 * t + e) * 4);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(q_empty);
@@ -526,14 +521,19 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
       const int left_keys = u.s.len - key0;   // keys of the tile that exist (a mask cuts the rest)
       const uint32_t tv = sb + stV * C::kTileBytes;
       // ---- the mask: key (relative to the tile) is seen iff key < hi and (key >= lo or key < snk)
+      // (tokens past the table see none of any tile)
       const int snk = p.sinks - key0;
-      const bool cut = key0 + kPage - 1 > pos_lo || (p.window > 0 && key0 <= pos_hi - p.window && snk < kPage);
+      const bool cut = key0 + kPage - 1 > pos_lo || pos_hi >= p.r.max_pages * kPage || (p.window > 0 && key0 <= pos_hi - p.window && snk < kPage);
       if (cut) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int hi = pos[nb][e] + 1 - key0;
+            // position of the row; below every key for rows past R or the table
+            const int r = 8 * nb + 2 * t + e;
+            int pos = r < R ? pos_lo + r / p.G : -1;
+            if (pos >= p.r.max_pages * kPage) pos = -1;
+            const int hi = pos + 1 - key0;
             const int lo = p.window > 0 ? hi - p.window : -kPage;
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)

@@ -126,8 +126,8 @@ __device__ __forceinline__ TilePlan tile_plan(const TileParams& p, int* mem, uns
     const int nb = (s.n + U - 1) / U;
     int tmax = 0;
     if (nb > 0) {
-      const int last = key_tiles_of(s.p0 + (nb - 1) * U, s.p0 + s.n, p.e.window, p.e.sinks).count();
-      const int first = key_tiles_of(s.p0, s.p0 + min(U, s.n), p.e.window, p.e.sinks).count();
+      const int last = key_tiles_of(s.p0 + (nb - 1) * U, s.p0 + s.n, p.e.window, p.e.sinks, p.key_tiles).count();
+      const int first = key_tiles_of(s.p0, s.p0 + min(U, s.n), p.e.window, p.e.sinks, p.key_tiles).count();
       // (under a window the blocks between may have one tile more than either)
       tmax = max(max(first, last) + (p.e.window > 0 && nb > 2 ? 1 : 0), 1);
       work += (unsigned long long)nb * (unsigned long long)(first + last);
@@ -247,7 +247,7 @@ __device__ __forceinline__ TileItem tile_item_of(const TileParams& p, int id, in
   it.s = s;
   it.tok0 = blk * 2 * p.TQ;
   const int first = s.p0 + it.tok0, end = s.p0 + min(it.tok0 + 2 * p.TQ, s.n);
-  it.kt = key_tiles_of(first, end, p.e.window, p.e.sinks);
+  it.kt = key_tiles_of(first, end, p.e.window, p.e.sinks, p.key_tiles);
   const int all = it.kt.count();
   it.lo = (int)((long long)all * part / parts);
   const int stop = (int)((long long)all * (part + 1) / parts);
@@ -741,7 +741,10 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::kThreadsT, 1)
       // positions: this row's, and the tile's first and last
       const int pos_lo = it.s.p0 + it.tok0 + X * p.TQ;
       const int pos_hi = pos_lo + p.TQ - 1;
-      const int pos = min_i(pos_lo + tr, it.s.len - 1);
+      int pos = min_i(pos_lo + tr, it.s.len - 1);
+      // tokens past the block table see no key: then every tile has a mask
+      const bool past = (min_i(pos_hi, it.s.p0 + it.s.n - 1) / kPage) >= p.key_tiles;
+      if (past && pos / kPage >= p.key_tiles) pos = -1;
       float m_ref = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++cnt) {
         if (!(ok = mbar_wait(bar(C::kBarS + X), (uint32_t)cnt & 1u, s_abort, status))) break;
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(TCfg<D, FP8>::kThreadsT, 1)
         tmem_wait_ld();
         const int key0 = (k_first + j + (k_first + j < k_sink ? 0 : k_skip)) * kPage;
         // the mask: keys after a row's position, and those before its window that are no sinks
-        const bool cut_hi = key0 + kPage - 1 > pos_lo;
+        const bool cut_hi = past || key0 + kPage - 1 > pos_lo;
         const bool cut_lo = WIN && key0 <= pos_hi - p.e.window && key0 + kPage > p.e.sinks;
         if (cut_hi) {
           const int hi = pos + 1 - key0;

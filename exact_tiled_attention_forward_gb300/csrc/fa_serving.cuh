@@ -20,10 +20,11 @@ struct Ragged {
 };
 
 // cu_seqlens and seqlens_k as the entry points define them: clamped, so that
-// no value they may hold leads out of the tensors.
+// no value they may hold leads out of the tensors. (A length of max_pages * 128 + T puts
+// all of a batch's tokens past the table, as any larger one does.)
 __device__ __forceinline__ int cu_at(const Ragged& r, int b) { return min(max(__ldg(r.cu + b), 0), r.T); }
 __device__ __forceinline__ int len_at(const Ragged& r, int b) {
-  return min(max(__ldg(r.lens + b), 0), r.max_pages * kPage);
+  return min(max(__ldg(r.lens + b), 0), r.max_pages * kPage + r.T);
 }
 // Page of table entry `i` of sequence b, -1 when it lies outside the cache.
 __device__ __forceinline__ int page_at(const Ragged& r, int b, int i) {
@@ -82,23 +83,25 @@ struct ExtendParams {
   int* status;
 };
 
-// The tiles of 128 keys that query positions [p0, p1) (p1 > p0) see: the sink
-// tiles [0, n_sink), then [lo, hi). Positions below 0 see nothing.
+// The tiles of 128 keys that query positions [p0, p1) (p1 > p0) see, of the first `tiles`: the
+// sink tiles [0, n_sink), then [lo, hi). Positions below 0 or past those tiles see nothing.
 struct KeyTiles {
   int n_sink, lo, hi;
   __device__ __forceinline__ int count() const { return n_sink + hi - lo; }
   __device__ __forceinline__ int tile(int k) const { return k < n_sink ? k : lo + (k - n_sink); }
 };
-__device__ __forceinline__ KeyTiles key_tiles_of(int p0, int p1, int window, int sinks) {
+__device__ __forceinline__ KeyTiles key_tiles_of(int p0, int p1, int window, int sinks, int tiles = 0x7FFFFFFF) {
+  if (p0 / kPage >= tiles) return KeyTiles{0, 0, 0};
   KeyTiles kt;
-  kt.hi = (max(p1, 0) + kPage - 1) / kPage;
+  kt.hi = min((max(p1, 0) + kPage - 1) / kPage, tiles);
   kt.lo = window > 0 ? min(max(p0 - window + 1, 0) / kPage, kt.hi) : 0;
   kt.n_sink = window > 0 ? min((sinks + kPage - 1) / kPage, kt.lo) : 0;
   return kt;
 }
 
 // Sequence b's new tokens: rows t0 .. t0 + n - 1 of the packed batch are computed
-// (n <= max_q); token t stands at position p0 + t; the sequence holds `len` keys.
+// (n <= max_q); token t stands at position p0 + t; the sequence holds `len` keys, or as
+// many as its table has room for.
 struct SeqTokens {
   int t0, n, p0, len;
 };
@@ -129,6 +132,7 @@ struct TileParams {
   int sms;             // SMs of the device
   int grid;            // CTAs of the launch: at least the items of any plan
   int kv_bytes;        // K and V bytes per key of one KV head
+  int key_tiles;       // tiles that the block table has room for (contiguous: no bound)
   int* cut;            // the plan's longest part, for the merge kernel
   int max_split_items; // 0: no key range is split
   long long o_b, o_t, o_h, o_g;   // element strides of o (lse: the same over d) by batch, token, KV head, query head

@@ -11,9 +11,11 @@
  *    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (its count n_b may be 0). Values
  *    are clamped to [0, T] and to be non-decreasing; rows from cu_seqlens[B]
  *    on are padding: not read, and left as they were in every output.
- *  - seqlens_k: int32 [B], device: sequence b's length L_b, its n_b new tokens
- *    included, clamped to [0, max_pages * 128]. New token t of sequence b (t =
- *    0 .. n_b - 1) stands at position L_b - n_b + t.
+ *  - seqlens_k: int32 [B], device: sequence b's length L_b (0 when negative), its
+ *    n_b new tokens included. New token t of sequence b (t = 0 .. n_b - 1) stands
+ *    at position L_b - n_b + t. A position below 0 or past the block table
+ *    (max_pages * 128 and on) is no place: a token there is not written, reads as
+ *    zeros, and sees no key.
  * The lengths live on the device, so a call captured into a CUDA graph follows
  * whatever they hold at each replay.
  *
@@ -50,7 +52,8 @@ typedef enum { FA_CACHE_16BIT = 0, FA_CACHE_E4M3 = 1 } fa_cache_format;
  * integer >= -120 with max|x| <= 448 * 2^e, codes = x * 2^-e rounded to nearest
  * even, byte = e + 127 (a row of zeros: codes 0, byte 7). A row that holds a NaN
  * or an infinity becomes a NaN row (byte 255, codes 0x7F). A token whose position
- * is below 0 or past the table is dropped. The new tokens of a batch must lie in
+ * is below 0 or past the table is dropped: a sequence that outgrows its table
+ * loses what no longer fits, and keeps what it holds. The new tokens of a batch must lie in
  * distinct cache rows (two sequences sharing a page they both write race).
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
 int fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, unsigned char* k_exp,
@@ -61,7 +64,8 @@ int fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, 
 /* Read rows back: k, v (dtype [T][H_kv][d], contiguous) receive what the cache
  * holds at the positions fa_cache_append would write (the last n_b of the first
  * L_b positions of each sequence; a whole sequence has n_b = L_b). E4M3 rows
- * come back as the values they stand for. A position below 0 gives zeros.
+ * come back as the values they stand for. A position below 0 or past the table gives
+ * zeros.
  * Returns as fa_cache_append. */
 int fa_cache_read(const void* k_cache, const void* v_cache, const unsigned char* k_exp,
                   const unsigned char* v_exp, const int* block_table, const int* cu_seqlens,
@@ -74,7 +78,8 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const unsigned char*
  *     j <= pos  and  (window == 0  or  j > pos - window  or  j < sinks),
  * i.e. everything before it, or its last `window` keys (itself among them) and the
  * sequence's first `sinks` keys. O = softmax(scale * Q K^T) V over them, LSE as
- * fa_forward's; a token that sees no key (pos < 0) gets O = 0 and LSE = -inf.
+ * fa_forward's; a token that sees no key (pos < 0 or past the table) gets O = 0 and
+ * LSE = -inf.
  *  - q: dtype [T][H_q][d], rows of one token contiguous, tokens q_stride elements
  *    apart (at least H_q * d, a multiple of 8), 16-byte aligned; H_q % H_kv == 0.
  *  - o: dtype [T][H_q][d]; lse: FP32 [T][H_q] or NULL; contiguous.
