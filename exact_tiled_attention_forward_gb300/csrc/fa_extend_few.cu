@@ -24,7 +24,8 @@
 // E4M3 caches: codes are widened to FP16 in registers (exact, one conversion per two
 // codes). Q goes to FP16 times a power of two per row that puts the row's maximum in
 // [2^14, 2^15): exact for all but elements 2^-29 below the maximum, which lose bits
-// 2^-39 below it. A key's power of two multiplies its FP32 score. A value's goes into
+// 2^-39 below it. A key's power of two multiplies its FP32 score (below 2^31 before: keys of up
+// to 2^105 stay in range however small the query was). A value's goes into
 // P, whose FP16 has no room for values of any size: a warp takes its keys of a tile in
 // bands. A band is the keys that some row sees whose exponent is at most 12 below the largest
 // one left, E; P' = 2^(s c - x) * 2^(ev - E + 14) with x the row's largest score in the band,
@@ -34,7 +35,7 @@
 // 2^12 of each other, the usual case, are one band and one pass.
 //
 // Measured (8 KV heads): one token of 16 sequences of 8192 keys, 4 heads a KV head, E4M3,
-// d = 128, 52 us (271 MB at 5.2 TB/s, 77 % of a copy's rate), two tokens of 8 heads 68 us; one
+// d = 128, 52 us (271 MB at 5.2 TB/s, 77 % of a copy's rate), two tokens of 8 heads 70 us; one
 // of 64 sequences, window 1024, FP16, d = 64, 38 us (132 MB at 3.5 TB/s: 1.7 units a CTA,
 // so starting, borders and merging weigh as much).
 #include "fa_serving.cuh"
@@ -508,7 +509,8 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float f = __uint_as_float(ld_shared_u8x(ek + 16 * mt + 8 * h) << 23);
+            // exp_factor, but infinite for a NaN row, whose codes are NaN
+            const float f = __uint_as_float(max(ld_shared_u8x(ek + 16 * mt + 8 * h) << 23, 0x00400000u));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               sacc[nb][mt][2 * h] *= f;

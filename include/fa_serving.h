@@ -90,7 +90,8 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const unsigned char*
  *    they may hold anything. In a page that some token sees a key of, a sequence's own
  *    K and V must be finite: a NaN or infinity in V there reaches rows that do not see
  *    its key as 0 * NaN. Queries do not reach one another.
- *  - BF16: |V| up to 2^59 (the running maximum may lag behind a row's by 2^48).
+ *  - BF16: |V| up to 2^59 (the running maximum may lag behind a row's by 2^48), and |K| up
+ *    to 2^105 in an E4M3 cache (queries are scaled up to 2^14 before their products).
  * FP32 accumulation, softmax statistics and LSE; P is rounded to 16 bits for P V; an
  * E4M3 cache is read as the values it stands for, exactly. Deterministic.
  * Rows that read one KV head ((H_q / H_kv) * max_q) of at most 16 take a kernel that

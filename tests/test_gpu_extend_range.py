@@ -160,3 +160,63 @@ def test_values_that_are_all_tiny(fa, form):
     p = Rows(new, [300, 90], hq, hkv, 128, "bf16", 67)
     p.v *= 2.0 ** -100
     p.check(fa)
+
+
+# ---- keys and queries of very different sizes, whose scores are ordinary
+@pytest.mark.parametrize("size", [60, 104])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", FORMS, ids=FORM_IDS)
+def test_huge_keys_under_tiny_queries(fa, form, d, size):
+    new, hq, hkv = form
+    p = Rows(new, [300, 90], hq, hkv, d, "bf16", 68)
+    p.k *= 2.0 ** size
+    p.q = bits(to_f64(p.q) * 2.0 ** -size, "bf16")
+    p.check(fa)
+
+
+@pytest.mark.parametrize("size", [60, 100])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", FORMS, ids=FORM_IDS)
+def test_tiny_keys_under_huge_queries(fa, form, d, size):
+    new, hq, hkv = form
+    p = Rows(new, [300, 90], hq, hkv, d, "bf16", 69)
+    p.k *= 2.0 ** -size
+    p.q = bits(to_f64(p.q) * 2.0 ** size, "bf16")
+    p.check(fa)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", FORMS, ids=FORM_IDS)
+def test_huge_keys_that_a_huge_query_does_not_meet(fa, form, d):
+    # products beyond FP32 where no column is shared: those scores are 0
+    new, hq, hkv = form
+    p = Rows(new, [300, 90], hq, hkv, d, "bf16", 70)
+    q = np.zeros_like(to_f64(p.q))
+    q[..., : d // 2] = 2.0 ** 100
+    p.q = bits(q, "bf16")
+    p.k[..., : d // 2] = 0.0
+    p.k[..., d // 2:] = 2.0 ** 104
+    p.check(fa)
+
+
+@pytest.mark.parametrize("byte", [0, 1, 3, 7])
+@pytest.mark.parametrize("form", FORMS, ids=FORM_IDS)
+def test_the_smallest_exponent_bytes(fa, form, byte):
+    # rows of another writer, below what fa_cache_append makes: still code * 2^(byte - 127)
+    new, hq, hkv = form
+    p = Rows(new, [300, 90], hq, hkv, 128, "bf16", 74)
+    rng = np.random.default_rng(byte)
+    b = p.b
+    codes = [rng.integers(0x30, 0x7E, b.cache_shape()).astype(np.uint8) for _ in range(2)]
+    kb, vb = (np.full(b.cache_shape()[:3], byte, np.uint8) for _ in range(2))
+    p.q = bits(rng.normal(size=to_f64(p.q).shape) * 2.0 ** (127 - byte - 13), "bf16")
+    o, lse = fa.fa_extend_paged(dev(p.q), dev(codes[0]), dev(codes[1]), dev(b.table), dev(b.cu), dev(b.lens), int(b.new.max()),
+                                scale=2.0 ** -5, k_exp=dev(kb), v_exp=dev(vb))
+    ks, vs = b.rows(S.row_values(codes[0], kb)), b.rows(S.row_values(codes[1], vb))
+    ro, rl, ra = S.extend_reference(to_f64(p.q), ks, vs, b.cu, b.lens, 2.0 ** -5)
+    # weights differ by any amount here: the 2^-27 of the largest is on the largest value, 448 * 2^byte
+    err = np.abs(o.double().cpu().numpy() - ro)
+    u = U_BF16 + U_ACC
+    floor = 300 * 2.0 ** -27 * 448 * 2.0 ** (byte - 127)
+    assert (err <= half_spacing(np.abs(ro) + u * ra + floor) + u * ra + floor + 2.0 ** -133).all(), float(err.max() / np.abs(ro).max())
+    assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-3 + 2.0 ** -20 * np.abs(rl).max()
