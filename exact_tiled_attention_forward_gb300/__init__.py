@@ -154,6 +154,26 @@ def _stream_ptr(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory that a call on `stream` (see _stream_ptr) writes. On another stream than the
+    current one it belongs to that stream, whose earlier work is all that may still use it,
+    and when it is dropped it stays untouched until the current stream, which will read
+    it, has passed that point too."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle = _stream_ptr(stream)
+    here = torch.cuda.current_stream(device)
+    if handle == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def _dims(q, k):
     B, H_q, N_q, d = q.shape
     Bk, H_kv, N_k, dk = k.shape
@@ -191,9 +211,9 @@ def fa_forward(q, k, v, causal: bool = False, scale: float | None = None, out=No
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H_q, N_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, H_q, N_q, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     st = lib().fa_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, N_q, N_k,
                           d, int(bool(causal)), float(scale), _stream_ptr(stream))
     _check(st, "fa_forward")
@@ -209,9 +229,9 @@ def fa_forward_fp16(q, k, v, causal: bool = False, scale: float | None = None, o
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H_q, N_q, d), dtype=torch.float16, device=q.device)
+        out = _empty((B, H_q, N_q, d), torch.float16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     st = lib().fa_forward_fp16(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, N_q,
                                N_k, d, int(bool(causal)), float(scale), _stream_ptr(stream))
     _check(st, "fa_forward_fp16")
@@ -237,9 +257,9 @@ def fa_forward_fp8(q, k, v, descale, causal: bool = False, scale: float | None =
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H_q, N_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, H_q, N_q, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     dq, dk, dv = (float(x) for x in descale)
     st = lib().fa_forward_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, N_q, N_k,
                               d, int(bool(causal)), float(scale), dq, dk, dv, _stream_ptr(stream))
@@ -365,9 +385,9 @@ def _backward(what, q, k, v, o, lse, do, mask, scale, dq, dk, dv, stream):
                   do=(do, qs), dq=(dq, qs), dk=(dk, ks), dv=(dv, ks))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(qs, dtype, q.device, stream) if dq is None else dq
+    dk = _empty(ks, dtype, q.device, stream) if dk is None else dk
+    dv = _empty(ks, dtype, q.device, stream) if dv is None else dv
     st = getattr(lib(), what)(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk),
                               _ptr(dv), B, H_q, H_kv, N_q, N_k, d, *mask, float(scale),
                               FA_DTYPE_FP16 if dtype == torch.float16 else FA_DTYPE_BF16,
@@ -399,9 +419,9 @@ def fa_forward_window(q, k, v, window: int, sinks: int = 0, scale: float | None 
     qs, ks = (B, H_q, N_q, d), (B, H_kv, N_k, d)
     _check_layout(what, q=(q, qs), k=(k, ks), v=(v, ks), out=(out, qs), lse=(lse, qs[:3]))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, dtype, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty(qs[:3], dtype=torch.float32, device=q.device)
+        lse = _empty(qs[:3], torch.float32, q.device, stream)
     st = lib().fa_forward_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, N_q, N_k, d,
                                  _int32(what, "window", window), _int32(what, "sinks", sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
                                  FA_DTYPE_FP16 if dtype == torch.float16 else FA_DTYPE_BF16, _stream_ptr(stream))
@@ -444,9 +464,9 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seqlens_k, causal: bool = 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, dtype, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     st = lib().fa_decode_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seqlens_k),
                                _ptr(out), _ptr(lse), B, H_q, H_kv, N_q, num_pages, block_table.shape[1], d,
                                int(bool(causal)), float(scale),
@@ -586,9 +606,9 @@ def fa_cache_read(k_cache, v_cache, block_table, cu_seqlens, seqlens_k, num_toke
                                                      cu_seqlens, seqlens_k, d)
     shape = (int(num_tokens), H_kv, d)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        k = _empty(shape, dtype, k_cache.device, stream)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=k_cache.device)
+        v = _empty(shape, dtype, k_cache.device, stream)
     for name, t in (("k", k), ("v", v)):
         if t.dtype != dtype:
             raise TypeError(f"{what}: {name} is {t.dtype}, expected {dtype}")
@@ -618,7 +638,7 @@ def fa_extend_paged(q, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, max
     elem, fmt, pages, H_kv, B, width = _cache_format(what, dtype, k_cache, v_cache, k_exp, v_exp, block_table,
                                                      cu_seqlens, seqlens_k, d)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _empty(shape, dtype, q.device, stream)
     else:
         if out.dtype != dtype:
             raise TypeError(f"{what}: out is {out.dtype}, expected {dtype}")
@@ -628,7 +648,7 @@ def fa_extend_paged(q, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, max
             raise TypeError(f"{what}: lse is {lse.dtype}, expected torch.float32")
         _check_layout(what, lse=(lse, shape[:2]))
     elif return_lse:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+        lse = _empty(shape[:2], torch.float32, q.device, stream)
     st = lib().fa_extend_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _at(k_exp), _at(v_exp),
                                block_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
                                _at(lse), B, T, _int32(what, "max_q", max_q), H_q, H_kv, pages, width, d,
@@ -650,9 +670,9 @@ def fa_forward_noalloc(q, k, v, causal: bool = False, scale: float | None = None
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H_q, N_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, H_q, N_q, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     st = lib().fa_forward_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv,
                                   N_q, N_k, d, int(bool(causal)), float(scale), _stream_ptr(stream))
     _check(st, "fa_forward_noalloc")
@@ -670,9 +690,9 @@ def fa_forward_cluster_multicast(q, k, v, causal: bool = False, scale: float | N
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H_q, N_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, H_q, N_q, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     l = lib_single_gpu()
     st = l.fa_forward_cluster_multicast(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv,
                                         N_q, N_k, d, int(bool(causal)), float(scale), _stream_ptr(stream))
@@ -706,12 +726,12 @@ def fa_naive_forward(q, k, v, causal: bool = False, scale: float | None = None, 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = torch.empty((B, H_q, N_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty((B, H_q, N_q, d), torch.bfloat16, q.device, stream)
     if lse is None and return_lse:
-        lse = torch.empty((B, H_q, N_q), dtype=torch.float32, device=q.device)
+        lse = _empty((B, H_q, N_q), torch.float32, q.device, stream)
     nbytes = fa_naive_workspace_bytes(B, H_q, N_q, N_k)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 16), torch.uint8, q.device, stream)
     st = lib().fa_naive_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, N_q,
                                 N_k, d, int(bool(causal)), float(scale), _ptr(workspace),
                                 workspace.numel() * workspace.element_size(), _stream_ptr(stream))
