@@ -19,8 +19,8 @@ struct Ragged {
   const int* table;    // [B][max_pages]
 };
 
-// cu_seqlens and seqlens_k as the entry points define them: clamped, so that
-// no value they may hold leads out of the tensors. (A length of max_pages * 128 + T puts
+// cu_seqlens and seqlens_k as the entry points define them: clamped, so that no value they
+// may hold leads out of the tensors (decreasing ones: counts are cut at 0 below). (A length of max_pages * 128 + T puts
 // all of a batch's tokens past the table, as any larger one does.)
 __device__ __forceinline__ int cu_at(const Ragged& r, int b) { return min(max(__ldg(r.cu + b), 0), r.T); }
 __device__ __forceinline__ int len_at(const Ragged& r, int b) {

@@ -8,9 +8,11 @@
  * --------------
  * B sequences; T token rows, the new tokens of all sequences packed in order:
  *  - cu_seqlens: int32 [B + 1], device: sequence b's new tokens are rows
- *    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (its count n_b may be 0). Values
- *    are clamped to [0, T] and to be non-decreasing; rows from cu_seqlens[B]
- *    on are padding: not read, and left as they were in every output.
+ *    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (its count n_b may be 0). Values are
+ *    clamped to [0, T]; rows before cu_seqlens[0] and from cu_seqlens[B] on are
+ *    padding: not read, and left as they were in every output. They must not
+ *    decrease: where they do, nothing outside the tensors is reached, but rows that
+ *    two sequences claim may hold either's result, and some may hold neither.
  *  - seqlens_k: int32 [B], device: sequence b's length L_b (0 when negative), its
  *    n_b new tokens included. New token t of sequence b (t = 0 .. n_b - 1) stands
  *    at position L_b - n_b + t. A position below 0 or past the block table
