@@ -432,7 +432,8 @@ def fa_forward_window(q, k, v, window: int, sinks: int = 0, scale: float | None 
 def fa_backward_window(q, k, v, o, lse, do, window: int, sinks: int = 0, scale: float | None = None, dq=None,
                        dk=None, dv=None, stream=None):
     """Gradients (dq, dk, dv) of ``fa_forward_window`` given its o and lse and the upstream
-    gradient do; tensors as ``fa_backward`` takes them."""
+    gradient do; tensors as ``fa_backward`` takes them. o and lse must be those of exactly
+    the keys that this call shows (not of a whole whose piece k and v are)."""
     what = "fa_backward_window"
     mask = _int32(what, "window", window), _int32(what, "sinks", sinks)
     return _backward(what, q, k, v, o, lse, do, mask, scale, dq, dk, dv, stream)
@@ -596,7 +597,7 @@ def fa_cache_read(k_cache, v_cache, block_table, cu_seqlens, seqlens_k, num_toke
     """Read the last ``cu_seqlens[b + 1] - cu_seqlens[b]`` of each sequence's first
     ``seqlens_k[b]`` positions back out of a paged cache, as ``(k, v)``, each
     ``[num_tokens, H_kv, d]`` of ``dtype`` (default: the cache's own type, BF16 for
-    E4M3 caches). See ``include/fa_serving.h``."""
+    E4M3 caches); rows of no sequence are not written. See ``include/fa_serving.h``."""
     import torch
     what = "fa_cache_read"
     if dtype is None:
@@ -628,7 +629,9 @@ def fa_extend_paged(q, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, max
     d]`` (tokens packed by ``cu_seqlens``; a token stride is allowed), the cache as
     ``fa_cache_append`` takes it, ``max_q`` the largest number of new tokens of a sequence.
     ``window > 0``: a token sees its last ``window`` keys and the first ``sinks``. Returns
-    ``(o, lse)``: ``[T, H_q, d]`` and FP32 ``[T, H_q]``. See ``include/fa_serving.h``."""
+    ``(o, lse)``: ``[T, H_q, d]`` and FP32 ``[T, H_q]``; rows of no sequence, and tokens past
+    ``max_q`` of one that has more, are not written (without ``out`` and ``lse`` they hold
+    anything). See ``include/fa_serving.h``."""
     import torch
     what = "fa_extend_paged"
     if q.dim() != 3:

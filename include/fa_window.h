@@ -30,7 +30,10 @@ int fa_forward_window(const void* q, const void* k, const void* v, void* o, floa
                       void* stream);
 
 /* Gradients of fa_forward_window, given its o and lse and the upstream gradient
- * dout: everything else as fa_backward. */
+ * dout: everything else as fa_backward. Unlike there, o and lse must be those of exactly
+ * the keys that this call shows each row: rowsum(dout * o) is put right by the row sums of
+ * dS over them, which are 0 for no other lse. Keys held in pieces, each with the lse of
+ * the whole, are fa_backward's case and not this one's. */
 int fa_backward_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
                        const void* dout, void* dq, void* dk, void* dv, int B, int H_q, int H_kv, int N_q,
                        int N_k, int d, int window, int sinks, float scale, int dtype, void* stream);
