@@ -423,7 +423,8 @@ def fa_forward_window(q, k, v, window: int, sinks: int = 0, scale: float | None 
     if lse is None and return_lse:
         lse = _empty(qs[:3], torch.float32, q.device, stream)
     st = lib().fa_forward_window(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H_q, H_kv, N_q, N_k, d,
-                                 _int32(what, "window", window), _int32(what, "sinks", sinks), 1.0 / math.sqrt(d) if scale is None else float(scale),
+                                 _int32(what, "window", window), _int32(what, "sinks", sinks),
+                                 1.0 / math.sqrt(d) if scale is None else float(scale),
                                  FA_DTYPE_FP16 if dtype == torch.float16 else FA_DTYPE_BF16, _stream_ptr(stream))
     _check(st, what)
     return out, lse

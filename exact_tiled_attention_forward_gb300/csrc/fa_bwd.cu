@@ -118,15 +118,6 @@ struct BwdCfg {
   static constexpr uint32_t kTmS = 0, kTmP = 128, kTmA = 256, kTmB = 384;
 };
 
-// 1-D bulk copy global -> shared, completion counted on an mbarrier (both
-// addresses 16-byte aligned, size a multiple of 16).
-__device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // Tensor-memory column of the packed 16-bit operand for K-step kk (16 rows or
 // keys): chunk kk / 4, its first 32 columns.
 __device__ __forceinline__ uint32_t packed_col(int kk) { return (uint32_t)(kk >> 2) * 64u + (uint32_t)(kk & 3) * 8u; }
@@ -398,7 +389,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const CUtensorMap& tmQ, const CUten
     if (!FA_DBG_OK(p.status, q0 + kT <= p.nq_pad && bhq < p.B * p.H_q)) return false;
     mbar_arrive_expect_tx(bar(C::kBarXFull + x), C::kTileBytes + C::kVecBytes);
     bwd_load_tile<D>(sb + C::kOffX + x * C::kTileBytes, tmQ, bar(C::kBarXFull + x), q0, bhq);
-    bulk_load_1d(sb + C::kOffD + x * C::kVecBytes, p.dsum + (size_t)bhq * p.nq_pad + q0, C::kVecBytes,
+    bulk_copy_1d(sb + C::kOffD + x * C::kVecBytes, p.dsum + (size_t)bhq * p.nq_pad + q0, C::kVecBytes,
                  bar(C::kBarXFull + x));
     return true;
   };
@@ -407,7 +398,7 @@ __device__ __forceinline__ void bwd_dkdv_cta(const CUtensorMap& tmQ, const CUten
     const int bhq = b * p.H_q + hk * p.G + hl;
     mbar_arrive_expect_tx(bar(C::kBarYFull + y), C::kTileBytes + C::kVecBytes);
     bwd_load_tile<D>(sb + C::kOffY + y * C::kTileBytes, tmdO, bar(C::kBarYFull + y), q0, bhq);
-    bulk_load_1d(sb + C::kOffLse + y * C::kVecBytes, p.lse2 + (size_t)bhq * p.nq_pad + q0, C::kVecBytes,
+    bulk_copy_1d(sb + C::kOffLse + y * C::kVecBytes, p.lse2 + (size_t)bhq * p.nq_pad + q0, C::kVecBytes,
                  bar(C::kBarYFull + y));
   };
   const uint32_t tmem = bwd_setup<D>(smem, warp, lane, [&] {
@@ -537,17 +528,16 @@ __device__ __forceinline__ void bwd_dkdv_cta(const CUtensorMap& tmQ, const CUten
                      n_steps > 0 ? make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3])
                                  : make_float4(0.f, 0.f, 0.f, 0.f));
           }
-          ok = false;   // (nothing more to store)
         }
       }
-      const size_t row = ((size_t)bhk * p.N_k + (valid ? key : 0)) * D;
-      if (!ok) {
-      } else
-      if (grp == 0)   // warpgroup 0 writes dV, warpgroup 1 dK
-        store_row<D, E>(tmem + lane_base + C::kTmA, static_cast<uint16_t*>(p.dv) + row, 1.f, n_steps == 0, valid);
-      else
-        store_row<D, E>(tmem + lane_base + C::kTmB, static_cast<uint16_t*>(p.dk) + row, p.scale, n_steps == 0,
-                        valid);
+      if (!WIN || parts == 1) {   // warpgroup 0 writes dV, warpgroup 1 dK
+        const size_t row = ((size_t)bhk * p.N_k + (valid ? key : 0)) * D;
+        if (grp == 0)
+          store_row<D, E>(tmem + lane_base + C::kTmA, static_cast<uint16_t*>(p.dv) + row, 1.f, n_steps == 0, valid);
+        else
+          store_row<D, E>(tmem + lane_base + C::kTmB, static_cast<uint16_t*>(p.dk) + row, p.scale, n_steps == 0,
+                          valid);
+      }
     }
   }
   tc_fence_before();
@@ -606,8 +596,8 @@ __device__ __forceinline__ void bwd_dq_cta(const CUtensorMap& tmQ, const CUtenso
     const size_t vo = (size_t)bhq * p.nq_pad + q0;
     mbar_arrive_expect_tx(bar(C::kBarRes), C::kTileBytes + 2 * C::kVecBytes);
     bwd_load_tile<D>(sb + C::kOffRes, tmQ, bar(C::kBarRes), q0, bhq);
-    bulk_load_1d(sb + C::kOffLse, p.lse2 + vo, C::kVecBytes, bar(C::kBarRes));
-    bulk_load_1d(sb + C::kOffD, p.dsum + vo, C::kVecBytes, bar(C::kBarRes));
+    bulk_copy_1d(sb + C::kOffLse, p.lse2 + vo, C::kVecBytes, bar(C::kBarRes));
+    bulk_copy_1d(sb + C::kOffD, p.dsum + vo, C::kVecBytes, bar(C::kBarRes));
     load_x(0);
     mbar_arrive_expect_tx(bar(C::kBarRes + 1), C::kTileBytes);
     bwd_load_tile<D>(sb + C::kOffRes + C::kTileBytes, tmdO, bar(C::kBarRes + 1), q0, bhq);
@@ -742,10 +732,11 @@ __device__ __forceinline__ void bwd_dq_cta(const CUtensorMap& tmQ, const CUtenso
             st_global_v4(dst + cc + 8 * g, pack2<E>(a[8 * g], a[8 * g + 1]), pack2<E>(a[8 * g + 2], a[8 * g + 3]),
                          pack2<E>(a[8 * g + 4], a[8 * g + 5]), pack2<E>(a[8 * g + 6], a[8 * g + 7]));
         }
-      } else
-      store_row<D, E>(tmem + lane_base + C::kTmB,
-                      static_cast<uint16_t*>(p.dq) + ((size_t)bhq * p.N_q + (valid ? row : 0)) * D, p.scale,
-                      n_steps == 0, valid, grp * (D / 2), (grp + 1) * (D / 2));
+      } else {
+        store_row<D, E>(tmem + lane_base + C::kTmB,
+                        static_cast<uint16_t*>(p.dq) + ((size_t)bhq * p.N_q + (valid ? row : 0)) * D, p.scale,
+                        n_steps == 0, valid, grp * (D / 2), (grp + 1) * (D / 2));
+      }
     }
   }
   tc_fence_before();

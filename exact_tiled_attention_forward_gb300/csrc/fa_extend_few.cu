@@ -108,14 +108,6 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 ld_shared_v4u(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 // Byte offset in a tile of 16-byte chunk `ch` of key row `key`, as TMA lays it out:
 // 16-bit tiles in 64-column boxes with the 128-byte swizzle; E4M3 rows of 128 bytes
@@ -525,7 +517,8 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
       // ---- the mask: key (relative to the tile) is seen iff key < hi and (key >= lo or key < snk)
       // (tokens past the table see none of any tile)
       const int snk = p.sinks - key0;
-      const bool cut = key0 + kPage - 1 > pos_lo || pos_hi >= p.r.max_pages * kPage || (p.window > 0 && key0 <= pos_hi - p.window && snk < kPage);
+      const bool cut = key0 + kPage - 1 > pos_lo || pos_hi >= p.r.max_pages * kPage ||
+                       (p.window > 0 && key0 <= pos_hi - p.window && snk < kPage);
       if (cut) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -778,7 +771,8 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, FP8, NB>::kPerSm)
     const bool whole = u.k0 == 0 && u.k1 == u.count;
     const int slot = 2 * blockIdx.x + (u.k0 == 0 ? 1 : 0);   // a unit cut at its end: slot 1; one that goes on: slot 0
     // the warps' O side by side in shared memory, 32 columns at a time, as many at once as
-    // the rows leave room for (one barrier before their sums and one after). A row's 16-byte chunks are XORed with the row against bank conflicts.
+    // the rows leave room for (one barrier before their sums and one after). A row's 16-byte
+    // chunks are XORed with the row against bank conflicts.
     const int at_once = R <= 4 ? 4 : R <= 8 ? 2 : 1;
     const uint32_t bufs = sb + C::kOffBuf;
     auto place = [&](int blk, int w, int m, int c4) {   // chunk c4 of row m of warp w

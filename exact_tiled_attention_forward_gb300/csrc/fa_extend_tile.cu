@@ -32,7 +32,7 @@
 //
 // Bound: the tensor cores over 16-bit caches; over E4M3 ones shared memory, which the codes
 // pass through twice more. Measured (32/8 heads, d = 128, BF16): 4096 new tokens of 32768
-// 1464 us (1410 TFLOP/s), 4 x 512 of 8192 167 us (1080), E4M3 2 x 2048, window 4096, 336 us
+// 1446 us (1425 TFLOP/s), 4 x 512 of 8192 163 us (1100), E4M3 2 x 2048, window 4096, 338 us
 // (790); fa_forward_window, N = 8192, window 1024, 145 us (890 over the pairs that see each
 // other, 20 % of the tiles' work lies outside).
 #include "fa_fwd_kernel.cuh"
@@ -346,11 +346,6 @@ __device__ __noinline__ void widen_slow(uint4 w, uint32_t byte, uint32_t* o) {
     const uint32_t f2 = kHalf ? pack_f16x2(g, g) : pack_bf16x2(g, g);
     for (int k = 0; k < 8; ++k) o[k] = mul_pair<E>(o[k], f2);
   }
-}
-__device__ __forceinline__ uint4 ld_shared_v4u(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
 }
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
   uint32_t v;

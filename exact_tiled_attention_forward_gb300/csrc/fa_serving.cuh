@@ -63,6 +63,15 @@ __device__ __forceinline__ void bulk_copy_1d(uint32_t dst, const void* src, uint
       : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4u(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // ---- attention of new tokens over the cache (fa_extend_paged)
 struct ExtendParams {
   Ragged r;
