@@ -99,6 +99,7 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const unsigned char*
  * Rows that read one KV head ((H_q / H_kv) * max_q) of at most 16 take a kernel that
  * streams the cache once at HBM rate; more take tcgen05 tiles of 128 rows. Over E4M3
  * pages a few chunks beside many sequences of a token or two take both, each its own.
+ * (One token a sequence over 16-bit pages, no window: fa_decode_paged is the leaner call.)
  * Returns FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED (d; H_q / H_kv > 128),
  * FA_ERR_NO_MEMORY or FA_ERR_CUDA. */
 int fa_extend_paged(const void* q, const void* k_cache, const void* v_cache, const unsigned char* k_exp,
