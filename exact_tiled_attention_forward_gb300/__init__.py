@@ -160,7 +160,7 @@ def _empty(shape, dtype, device, stream):
     and when it is dropped it stays untouched until the current stream, which will read
     it, has passed that point too."""
     import torch
-    if stream is None:
+    if stream is None or device.type != "cuda":   # (libfa refuses what is not on the device)
         return torch.empty(shape, dtype=dtype, device=device)
     handle = _stream_ptr(stream)
     here = torch.cuda.current_stream(device)
